@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas) k_token_logprobs_grad
 
 template <typename T, int TH>
 int launch_logprobs(LogprobArgs a, int cluster, cudaStream_t s) {
+    static_assert(kUnaskedSmem + sizeof(StatSmem) + sizeof(TopSmem) <= 48 * 1024, "static shared memory");
     if (a.K == 0) return launch_rows(k_token_logprobs<T, TH, false>, cluster, a.row.N, TH, 0, a, s);
     return launch_rows(k_token_logprobs<T, TH, true>, cluster, a.row.N, TH,
                        top_bytes(a.K, cluster, TH, most_units(a.row.part, TH)), a, s);
