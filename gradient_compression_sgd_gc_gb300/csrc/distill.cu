@@ -427,8 +427,8 @@ int launch_loss(DistillArgs a, cudaStream_t s) {
     if (sms < 1) return GC_ERR_CUDA;
     const StreamGeometry g = stream_geometry(a.row.N, a.row.V, sizeof(T), 0, sms);
     a.row.part = g.part;
-    return g.threads == 128 ? launch_rows(k_distill_loss<T, 128>, g.cluster, a.row.N, 128, 0, a, s)
-                            : launch_rows(k_distill_loss<T, 256>, g.cluster, a.row.N, 256, 0, a, s);
+    return g.threads == 128 ? launch_rows(k_distill_loss<T, 128>, g.cluster, a.row.N, 128, 0, 0, a, s)
+                            : launch_rows(k_distill_loss<T, 256>, g.cluster, a.row.N, 256, 0, 0, a, s);
 }
 
 // The part of a row that a CTA works on at most: 608 parts of 87 KB (a row of
@@ -451,7 +451,7 @@ int launch_loss_grad(DistillArgs a, cudaStream_t s) {
     while (cluster < kMaxCluster && bytes > cluster * kStepPartBytes) ++cluster;
     while (cluster * 2 <= kMaxCluster && a.row.N <= sms / (cluster * 2) && bytes > cluster * 2 * kMinStepPartBytes) cluster *= 2;
     a.row.part = static_cast<int>((bytes / 16 + cluster - 1) / cluster);
-    return launch_rows(k_distill_loss_grad<T>, cluster, a.row.N, kTeacherThreads, 0, a, s);
+    return launch_rows(k_distill_loss_grad<T>, cluster, a.row.N, kTeacherThreads, 0, 0, a, s);
 }
 
 DistillArgs distill_args(const void* logits, int64_t ld, const int32_t* top_ids, const float* top_logits, int K, int64_t N,

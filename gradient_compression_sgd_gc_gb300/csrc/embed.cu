@@ -872,11 +872,13 @@ int launch_sum(const GradArgs& a, bool vec, cudaStream_t s) {
     const unsigned blocks = static_cast<unsigned>((a.nseg * a.chunks + kWarpsPerBlock - 1) / kWarpsPerBlock);
     const int smem = kWarpsPerBlock * kRing * kPlace * static_cast<int>(sizeof(TI));
     auto kernel = vec ? k_embed_sum<TI, TO, true> : k_embed_sum<TI, TO, false>;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return GC_ERR_CUDA;
+    if (allow_smem(kernel, smem, smem) != GC_OK) return GC_ERR_CUDA;
     return launch_next(kernel, blocks, kThreads, smem, a, s);
 }
+
+// Shared memory of a sorting CTA whose class has `ids` ids: counts of each warp,
+// and where each id's tokens begin.
+constexpr size_t order_bytes(int64_t ids) { return ((kSortWarps + 1) * ids + 1) * sizeof(int); }
 
 // Whether every row of p starts on a boundary of 8 elements.
 bool rows_aligned(const void* p, int64_t ld, int type) { return aligned_to(p, 8 * type_bytes(type)) && ld % 8 == 0; }
@@ -970,10 +972,9 @@ int embed_grad(const void* dout, gc_dtype dout_type, int64_t ld_dout, const void
     a.piece_pitch = ld_dtable == D ? kPieceBytes : ld_dtable * a.elem;
     a.pieces = (a.zero_bytes + a.piece_pitch - 1) / a.piece_pitch;
     const int zero_ctas = static_cast<int>(std::min<int64_t>(kZeroCtas, a.pieces));
-    const int smem = std::max<int>(kPieceBytes, ((kSortWarps + 1) * static_cast<int>(a.classes.each + 1) + 1) * static_cast<int>(sizeof(int)));
+    const size_t smem = std::max<size_t>(kPieceBytes, order_bytes(a.classes.each + 1));
     auto order = tiled ? k_embed_order<int, true> : a.id64 ? k_embed_order<long long, false> : k_embed_order<int, false>;
-    if (cudaFuncSetAttribute(order, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return GC_ERR_CUDA;
+    if (allow_smem(order, smem, order_bytes(kMaxRange + 1)) != GC_OK) return GC_ERR_CUDA;
     if (tiled) {
         auto tiles = a.id64 ? k_embed_tiles<long long> : k_embed_tiles<int>;
         tiles<<<static_cast<unsigned>(a.tiles), kTileThreads, kTileWarps * B * sizeof(int), s>>>(a);

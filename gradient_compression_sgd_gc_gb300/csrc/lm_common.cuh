@@ -19,6 +19,26 @@ inline size_t type_bytes(int t) { return t == GC_F32 ? 4 : 2; }
 inline bool valid_temperature(double t) { return t >= 1e-6 && t <= 1e6; }
 inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// ---------------------------------------------------------------- shared memory
+
+// The dynamic shared memory that a kernel gets without asking: 48 KB less its
+// static memory, for which 4 KB are left.
+constexpr size_t kUnaskedSmem = 44 * 1024;
+
+// Lets launches of `kernel` have `smem` bytes of dynamic shared memory.  The
+// limit belongs to the kernel on the device, not to the call: another host
+// thread may be between asking and launching, so every call asks for the same,
+// the most that the kernel ever takes.
+template <typename Kernel>
+int allow_smem(Kernel* kernel, size_t smem, size_t most) {
+    if (smem > kUnaskedSmem && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    static_cast<int>(most)) != cudaSuccess) {
+        cudaGetLastError();
+        return GC_ERR_CUDA;
+    }
+    return GC_OK;
+}
+
 // ---------------------------------------------------------------- elements
 
 // A 16-byte vector holds E elements of T, read and written as floats.

@@ -307,18 +307,13 @@ __device__ __forceinline__ float row_lse(const Stat& st, float ln_s, const RowAr
 
 // ---------------------------------------------------------------- launch
 
-// The dynamic shared memory that a kernel gets without asking: 48 KB less its
-// static memory, for which 4 KB are left.
-constexpr size_t kUnaskedSmem = 44 * 1024;
-
-// Launches `clusters` clusters of `cluster` CTAs.
+// Launches `clusters` clusters of `cluster` CTAs with `smem` bytes of dynamic
+// shared memory each, of `most` that the kernel ever takes.
 template <typename Args>
-int launch_rows(void (*kernel)(Args), int cluster, int64_t clusters, int threads, size_t smem, const Args& a,
+int launch_rows(void (*kernel)(Args), int cluster, int64_t clusters, int threads, size_t smem, size_t most, const Args& a,
                 cudaStream_t s) {
     if (clusters > 0x7fffffffLL / cluster) return GC_ERR_INVALID;
-    if (smem > kUnaskedSmem &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return GC_ERR_CUDA;
+    if (allow_smem(kernel, smem, most) != GC_OK) return GC_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
     cfg.blockDim = dim3(threads);

@@ -37,7 +37,7 @@ struct Units {
 };
 
 // Most units that a part of `vectors` vectors has.
-inline int most_units(int vectors, int threads) { return vectors / (kBatch * threads) + 2; }
+constexpr int most_units(int vectors, int threads) { return vectors / (kBatch * threads) + 2; }
 
 // The thread's statistics over its units; note(u, m) is called with each
 // unit's largest entry.  The next unit's vectors are read into registers

@@ -65,10 +65,14 @@ struct TopBuffers {
     }
 };
 
-inline size_t top_bytes(int K, int parts, int threads, int units) {
+constexpr size_t top_bytes(int K, int parts, int threads, int units) {
     return sizeof(uint64_t) * (candidate_cap(K) + kPad + static_cast<size_t>(parts) * K) + sizeof(uint32_t) * hit_cap(K) +
            sizeof(uint16_t) * threads * units;
 }
+
+// More than any call takes: the most alternatives in the largest cluster, with
+// the units of a whole fp32 row of the longest (whose CTAs have 256 threads).
+constexpr size_t kMostTopBytes = top_bytes(GC_MAX_TOP, kMaxCluster, 256, most_units(GC_MAX_VOCAB / 4 + 2, 256));
 
 // Calls f(key, index) for every entry of the part, by the thread that has it.
 template <int TH, typename T, typename F>
@@ -423,9 +427,9 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas) k_token_logprobs_grad
 template <typename T, int TH>
 int launch_logprobs(LogprobArgs a, int cluster, cudaStream_t s) {
     static_assert(kUnaskedSmem + sizeof(StatSmem) + sizeof(TopSmem) <= 48 * 1024, "static shared memory");
-    if (a.K == 0) return launch_rows(k_token_logprobs<T, TH, false>, cluster, a.row.N, TH, 0, a, s);
+    if (a.K == 0) return launch_rows(k_token_logprobs<T, TH, false>, cluster, a.row.N, TH, 0, 0, a, s);
     return launch_rows(k_token_logprobs<T, TH, true>, cluster, a.row.N, TH,
-                       top_bytes(a.K, cluster, TH, most_units(a.row.part, TH)), a, s);
+                       top_bytes(a.K, cluster, TH, most_units(a.row.part, TH)), kMostTopBytes, a, s);
 }
 
 template <typename T>

@@ -797,7 +797,8 @@ GC_API int saps_mask_compact_noalloc(int64_t n, double p, uint64_t seed_t,
  * nothing but -inf has no distribution: its lse, and every log probability in
  * it, is -inf, its entropy 0, every probability 0.  A row with a NaN or +inf
  * has NaN for all of these.  Every result is a fixed function of the inputs
- * and the device (no floating-point atomics).
+ * and the device (no floating-point atomics).  The calls of this section may
+ * come from several host threads at once; each needs buffers of its own.
  */
 
 /* Token id type. */
