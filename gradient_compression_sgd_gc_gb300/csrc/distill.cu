@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kTeacherThreads, kGradCtas) k_distill_grad(Dis
         if (in_place) gather();             // before any of them is overwritten
     }
     __syncthreads();
-    const bool zero = weight == 0.0f || !teacher.mass, usual = fabsf(lse) < -kFloor;
+    const bool zero = weight == 0.0f || !teacher.mass, usual = may_floor(lse, inv_tau);
     // log p = y - lse in natural units, so that neither the rounding of
     // lse * log2(e) nor that of 1 / tau scales the row
     auto prob = [&](float x) {

@@ -169,6 +169,14 @@ __device__ __forceinline__ void raise(Sums& st, float m, float c2) {
 constexpr float kFloor = -1152921504606846976.0f;
 constexpr uint32_t kFloorBf16x2 = 0xdd80dd80u;
 
+// Whether a row with this lse may have everything below -2^60 raised to it.  lse
+// counts in units of x / tau: with tau > 1 a row whose largest logit is below
+// -2^60 can have an lse above it.  Where this holds the largest logit is above
+// -2^59, so a raised entry is 2^59 / tau below it and its power zero.
+__device__ __forceinline__ bool may_floor(float lse, float inv_tau) {
+    return fabsf(lse) < -0.5f * kFloor * fminf(1.0f, inv_tau);
+}
+
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

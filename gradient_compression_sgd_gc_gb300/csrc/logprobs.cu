@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas) k_token_logprobs_grad
     const float token = g * inv_tau;
     const float k1 = -h * inv_tau, k0 = fmaf(k1, H, id >= 0 ? -token : 0.0f);
     const int v_id = id >= 0 ? static_cast<int>((id + p.shift) / E) : -1;
-    const bool usual = fabsf(lse) < -kFloor;
+    const bool usual = may_floor(lse, inv_tau);
     T* out = static_cast<T*>(a.out) + n * a.ld_out;
     stream_map<kGradThreads>(p, out, [&](int v, uint4 w) {
         float f[E];
