@@ -226,9 +226,52 @@ constexpr int kStepCtas = 4;                // resident per SM
 __device__ __forceinline__ void rows_arrive() { asm volatile("bar.arrive 1, %0;" ::"n"(kTeacherThreads) : "memory"); }
 __device__ __forceinline__ void teacher_wait() { asm volatile("bar.sync 1, %0;" ::"n"(kTeacherThreads) : "memory"); }
 
+// Writes g p = gs 2^(c2 (x - m)) over a part of a row; zeros where it has none.
+template <typename T>
+__device__ __forceinline__ void map_gradient(const RowPart<T>& p, T* out, bool none, float gs, float m, float c2) {
+    constexpr int E = Elem<T>::E;
+    const uint64_t minus_m = pair(-m, -m), cc = pair(c2, c2), gg = pair(gs, gs);
+    stream_map<kRowThreads>(p, out, [&](int, uint4 x) {
+        if (none) return make_uint4(0, 0, 0, 0);
+        float f[E];
+        Elem<T>::unpack(x, f);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            float y0, y1;
+            unpair(pair_mul(pair_add(pair(f[e], f[e + 1]), minus_m), cc), y0, y1);
+            unpair(pair_mul(pair(exp2_fast(y0), exp2_fast(y1)), gg), f[e], f[e + 1]);
+        }
+        return Elem<T>::pack(f);
+    });
+}
+
+// The gradients g p - g q at the part's entries, whose logits are x, after the
+// part's threads have written theirs.  By the teacher's warp.
+template <typename T, typename P>
+__device__ __forceinline__ void correct_entries(const Own& own, int n_own, bool zero, const float (&x)[GC_MAX_TOP / 32], T* out,
+                                                float g, P g_prob) {
+    constexpr int kPer = GC_MAX_TOP / 32;
+    const int lane = threadIdx.x & 31;
+    float fix[kPer];
+    bool first[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int k = lane + 32 * i;
+        first[i] = false;
+        if (k < n_own && !zero) {
+            const float q = merged_q(own, k, n_own);
+            first[i] = !(q < 0.0f);
+            fix[i] = fmaf(-g, q, g_prob(x[i]));
+        }
+    }
+    teacher_wait();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (first[i]) out[own.id[lane + 32 * i]] = Elem<T>::round_to(fix[i]);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kTeacherThreads, kStepCtas) k_distill_loss_grad(DistillArgs a) {
-    constexpr int E = Elem<T>::E;
     constexpr int kPer = GC_MAX_TOP / 32;
     __shared__ StatSmem stat_smem;
     __shared__ Teacher teacher;
@@ -271,42 +314,15 @@ __global__ void __launch_bounds__(kTeacherThreads, kStepCtas) k_distill_loss_gra
     const float gs = none ? 0.0f : g / st.s;
     T* out = static_cast<T*>(a.out) + n * a.ld_out;
     if (rows) {
-        const uint64_t minus_m = pair(-st.m, -st.m), cc = pair(c2, c2), gg = pair(gs, gs);
-        stream_map<kRowThreads>(p, out, [&](int, uint4 x) {
-            if (none) return make_uint4(0, 0, 0, 0);
-            float f[E];
-            Elem<T>::unpack(x, f);
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                float y0, y1;
-                unpair(pair_mul(pair_add(pair(f[e], f[e + 1]), minus_m), cc), y0, y1);
-                unpair(pair_mul(pair(exp2_fast(y0), exp2_fast(y1)), gg), f[e], f[e + 1]);
-            }
-            return Elem<T>::pack(f);
-        });
+        map_gradient(p, out, none, gs, st.m, c2);
         rows_arrive();
     } else {
         if (rank == 0) {
             const float loss = row_loss(teacher, x_all, st, logf(st.s), a);
             if (lane == 0) a.loss[n] = loss;
         }
-        float fix[kPer];
-        bool first[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int k = lane + 32 * i;
-            first[i] = false;
-            if (k < n_own && !zero) {
-                const float q = merged_q(own, k, n_own);
-                first[i] = !(q < 0.0f);
-                const float s = none ? 0.0f : gs * exp2_fast(exponent(x_own[i], st.m, c2));
-                fix[i] = fmaf(-g, q, s);
-            }
-        }
-        teacher_wait();                     // the entries' corrections come after the row
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (first[i]) out[own.id[lane + 32 * i]] = Elem<T>::round_to(fix[i]);
+        correct_entries(own, n_own, zero, x_own, out, g,
+                        [&](float x) { return none ? 0.0f : gs * exp2_fast(exponent(x, st.m, c2)); });
     }
 }
 
@@ -329,53 +345,88 @@ struct DistillGradArgs {
     int* status;
 };
 
-// One CTA per piece of a row, with a warp of its own for the teacher's entries.
+// The teacher's side of a part, by its warp; the entries that lie in it are counted in n_own.
 template <typename T>
-__global__ void __launch_bounds__(kTeacherThreads, kGradCtas) k_distill_grad(DistillGradArgs a) {
+struct PartEntries {
+    float x[GC_MAX_TOP / 32];               // the student's logits at the part's entries
+    int n_own;
+
+    __device__ __forceinline__ void find(const DistillGradArgs& a, int64_t n, const RowPart<T>& p, Teacher& teacher, Own& own,
+                                         int* status) {
+        load_teacher(teacher, a.top_ids + n * a.K, a.top_logits + n * a.K, a.K, a.row.V, a.row.c2, status);
+        __syncwarp();
+        n_own = collect_own(own, teacher, a.K, p.index(p.v0, 0), p.index(p.v1, 0));
+    }
+
+    __device__ __forceinline__ void gather(const RowPart<T>& p, const Own& own) {
+#pragma unroll
+        for (int i = 0; i < GC_MAX_TOP / 32; ++i) {
+            const int k = (threadIdx.x & 31) + 32 * i;
+            if (k < n_own) x[i] = Elem<T>::load_plain(p.row + own.id[k]);
+        }
+    }
+};
+
+// The gradient of a row whose lse does not hold its sum, by one CTA: the row is
+// read once more before, and nothing is written until then, so it may be in
+// place.  2048 x 131072 bf16 of -1e9 with 64 entries take 245 us, where usual
+// rows take 163; 300 x 50001 fp32 36 and 20.
+template <typename T>
+__device__ __noinline__ void whole_row_grad(const DistillGradArgs& a, int64_t n, Teacher& teacher, Own& own) {
+    __shared__ StatSmem stat_smem;
+    const RowPart<T> p(a.row, n, 0, kWholeRow);
+    const bool rows = threadIdx.x < kRowThreads;
+    const float c2 = a.row.c2, g = __ldg(a.weights + n) * a.tau;
+    T* out = static_cast<T*>(a.out) + n * a.ld_out;
+    PartEntries<T> entries;
+    if (!rows) {
+        entries.find(a, n, p, teacher, own, a.status);
+        entries.gather(p, own);
+    }
+    const Stat st = whole_row_stats<kRowThreads>(p, stat_smem, c2);
+    const bool zero = !teacher.mass, none = zero || st.m == neg_inf();
+    const float gs = none ? 0.0f : g / st.s;
+    if (rows) {
+        map_gradient(p, out, none, gs, st.m, c2);
+        rows_arrive();
+    } else {
+        correct_entries(own, entries.n_own, zero, entries.x, out, g,
+                        [&](float x) { return none ? 0.0f : gs * exp2_fast(exponent(x, st.m, c2)); });
+    }
+}
+
+// One CTA per piece of a row, or one for a row whose lse does not hold its sum,
+// with a warp of its own for the teacher's entries.
+template <typename T>
+__global__ void __launch_bounds__(kTeacherThreads, kGradCtas) k_distill_grad(const __grid_constant__ DistillGradArgs a) {
     constexpr int E = Elem<T>::E;
-    constexpr int kPer = GC_MAX_TOP / 32;
     __shared__ Teacher teacher;
     __shared__ __align__(16) Own own;
     const int64_t n = blockIdx.x / a.tiles;
     const unsigned tile = blockIdx.x % a.tiles;
+    const float lse = __ldg(a.lse + n), weight = __ldg(a.weights + n), inv_tau = a.row.inv_tau;
     const RowPart<T> p(a.row, n, tile);
     T* out = static_cast<T*>(a.out) + n * a.ld_out;
     const bool rows = threadIdx.x < kRowThreads, in_place = a.out == a.row.x;
-    const int lane = threadIdx.x & 31;
-    const float lse = __ldg(a.lse + n), weight = __ldg(a.weights + n), inv_tau = a.row.inv_tau;
     const float g = weight * a.tau;
-    float x_own[kPer];
-    int n_own = 0;
-    auto gather = [&]() {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (lane + 32 * i < n_own) x_own[i] = Elem<T>::load_plain(p.row + own.id[lane + 32 * i]);
-    };
+    PartEntries<T> entries;
     if (!rows) {
-        load_teacher(teacher, a.top_ids + n * a.K, a.top_logits + n * a.K, a.K, a.row.V, a.row.c2,
-                     tile == 0 ? a.status : nullptr);
-        __syncwarp();
-        n_own = collect_own(own, teacher, a.K, p.index(p.v0, 0), p.index(p.v1, 0));
-        if (in_place) gather();             // before any of them is overwritten
+        entries.find(a, n, p, teacher, own, tile == 0 ? a.status : nullptr);
+        if (in_place) entries.gather(p, own);           // before any of them is overwritten
     }
     __syncthreads();
-    const bool zero = weight == 0.0f || !teacher.mass, usual = may_floor(lse, inv_tau);
+    if (!lse_holds(lse) && weight != 0.0f) {            // without a weight all are zeros
+        if (tile == 0) whole_row_grad<T>(a, n, teacher, own);
+        return;
+    }
+    const bool zero = weight == 0.0f || !teacher.mass;
     // log p = y - lse in natural units, so that neither the rounding of
     // lse * log2(e) nor that of 1 / tau scales the row
-    auto prob = [&](float x) {
-        return lse == neg_inf() ? 0.0f : exp2_fast(log_prob_from(x, lse, inv_tau, a.inv_tau_low) * kLog2e);
-    };
     if (rows) {
         stream_map<kRowThreads>(p, out, [&](int, uint4 w) {
             float f[E];
             if (zero) return make_uint4(0, 0, 0, 0);
-            if (!usual) {                   // nothing but masked entries (p = 0), huge logits, or NaN
-                Elem<T>::unpack(w, f);
-#pragma unroll
-                for (int e = 0; e < E; ++e) f[e] = g * prob(f[e]);
-                return Elem<T>::pack(f);
-            }
-            Elem<T>::unpack(floored<T>(w), f);      // masked entries at -2^60: p is 0
+            Elem<T>::unpack(floored<T>(w), f);          // masked entries at -2^60: p is 0
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
                 const uint64_t lp = log_prob_pair(pair(f[e], f[e + 1]), lse, inv_tau, a.inv_tau_low);
@@ -387,23 +438,9 @@ __global__ void __launch_bounds__(kTeacherThreads, kGradCtas) k_distill_grad(Dis
         });
         rows_arrive();
     } else {
-        if (!in_place) gather();
-        float fix[kPer];
-        bool first[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int k = lane + 32 * i;
-            first[i] = false;
-            if (k < n_own && !zero) {
-                const float q = merged_q(own, k, n_own);
-                first[i] = !(q < 0.0f);
-                fix[i] = g * (prob(x_own[i]) - q);
-            }
-        }
-        teacher_wait();                     // the entries' corrections come after the piece
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (first[i]) out[own.id[lane + 32 * i]] = Elem<T>::round_to(fix[i]);
+        if (!in_place) entries.gather(p, own);
+        correct_entries(own, entries.n_own, zero, entries.x, out, g,
+                        [&](float x) { return g * exp2_fast(log_prob_from(x, lse, inv_tau, a.inv_tau_low) * kLog2e); });
     }
 }
 

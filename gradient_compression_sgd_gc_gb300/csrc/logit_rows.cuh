@@ -76,6 +76,8 @@ __device__ __forceinline__ void st_remote(uint32_t addr, uint64_t v) {
 
 // ---------------------------------------------------------------- the part of a row
 
+constexpr int kWholeRow = 1 << 30;          // vectors: a part that holds any row
+
 // A row starts anywhere, so its 16-byte vectors are counted from the aligned
 // address at or below its start: the first and the last may have lanes outside
 // the row ("ragged"), which are read by element and hold -inf.  A CTA has the
@@ -86,13 +88,16 @@ struct RowPart {
     const T* row;
     int V, shift, v0, v1, i0, i1;
 
-    __device__ __forceinline__ RowPart(const RowArgs& a, int64_t n, unsigned rank) {
+    __device__ __forceinline__ RowPart(const RowArgs& a, int64_t n, unsigned rank) : RowPart(a, n, rank, a.part) {}
+
+    // The same with other parts than the launch's, of `part` vectors.
+    __device__ __forceinline__ RowPart(const RowArgs& a, int64_t n, unsigned rank, int part) {
         row = static_cast<const T*>(a.x) + n * a.ld;
         V = a.V;
         shift = row_shift(row);
         const int last = (shift + V - 1) / E;
-        v0 = min(static_cast<int>(rank) * a.part, last + 1);
-        v1 = min(v0 + a.part, last + 1);
+        v0 = min(static_cast<int>(rank) * part, last + 1);
+        v1 = min(v0 + part, last + 1);
         i0 = v0, i1 = v1;
         if (v0 < v1) {
             if (v0 == 0 && shift != 0) i0 = 1;
@@ -169,13 +174,12 @@ __device__ __forceinline__ void raise(Sums& st, float m, float c2) {
 constexpr float kFloor = -1152921504606846976.0f;
 constexpr uint32_t kFloorBf16x2 = 0xdd80dd80u;
 
-// Whether a row with this lse may have everything below -2^60 raised to it.  lse
-// counts in units of x / tau: with tau > 1 a row whose largest logit is below
-// -2^60 can have an lse above it.  Where this holds the largest logit is above
-// -2^59, so a raised entry is 2^59 / tau below it and its power zero.
-__device__ __forceinline__ bool may_floor(float lse, float inv_tau) {
-    return fabsf(lse) < -0.5f * kFloor * fminf(1.0f, inv_tau);
-}
+// Whether a gradient may form log p as x / tau - lse.  lse is rounded to fp32: at
+// 1024 that is 2^-15 of p, and at 1e9 nothing of the sum's logarithm is left (a
+// row of one value would have p = 1 in every place).  Other rows, NaN and the
+// infinities among them, need their own maximum and sum.  Below 1024 the largest
+// logit is above -1024 tau, so a power that was raised to -2^60 is zero.
+__device__ __forceinline__ bool lse_holds(float lse) { return fabsf(lse) < 1024.0f; }
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;

@@ -89,6 +89,15 @@ __device__ __forceinline__ Stat stream_stats(const RowPart<T>& p, const Units<TH
     return finish(st);
 }
 
+// The statistics of a whole row that is not kept, the same in every thread of a
+// CTA; TH threads read, those above take part in the barriers alone.
+template <int TH, typename T>
+__device__ __forceinline__ Stat whole_row_stats(const RowPart<T> p, StatSmem& sm, float c2) {
+    Stat mine{neg_inf(), 0.0f, 0.0f};
+    if (threadIdx.x < TH) mine = stream_stats<TH, false, true>(p, Units<TH>(p), c2, [](int, float) {});
+    return block_stats<TH>(sm, mine, c2);
+}
+
 // Writes f(v, vector v) to the same places of `out` for every vector of the
 // part, the next unit's vectors read before the present one's arithmetic.
 // `out` may be the row itself.  Threads below TH call it.

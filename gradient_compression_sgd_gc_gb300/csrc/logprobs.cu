@@ -374,52 +374,91 @@ struct LogprobGradArgs {
     int* status;
 };
 
-// One CTA per piece of a row.
+// What a row's gradient is made of: d = p (k0 + k1 log p), and `token` more for
+// the token.
+template <typename T>
+struct Slope {
+    int64_t id;
+    float token, k0, k1;
+
+    __device__ __forceinline__ Slope(const LogprobGradArgs& a, int64_t n, bool entropy, int* status) {
+        id = load_id(a.ids, a.id64, n, a.row.V, status);
+        const float g = a.g_logprobs ? __ldg(a.g_logprobs + n) : 0.0f;
+        const float h = entropy ? __ldg(a.g_entropy + n) : 0.0f;
+        const float H = entropy ? __ldg(a.entropy + n) : 0.0f;
+        token = g * a.row.inv_tau;
+        k1 = -h * a.row.inv_tau;
+        k0 = fmaf(k1, H, id >= 0 ? -token : 0.0f);
+    }
+
+    // The vector that holds the token, -1 without one.
+    __device__ __forceinline__ int vector(const RowPart<T>& p) const {
+        return id >= 0 ? static_cast<int>((id + p.shift) / Elem<T>::E) : -1;
+    }
+
+    __device__ __forceinline__ void add_token(const RowPart<T>& p, int v, float (&f)[Elem<T>::E]) const {
+#pragma unroll
+        for (int e = 0; e < Elem<T>::E; ++e)
+            if (p.index(v, e) == id) f[e] += token;
+    }
+};
+
+// The gradient of a row whose lse does not hold its sum, by one CTA: the row is
+// read once more before, and nothing is written until then, so it may be in
+// place.  2048 x 131072 bf16 of -1e9 take 280 us, where usual rows take 162; 300
+// x 50001 fp32 34 and 19; one row of 131072 bf16 25 and 9.
 template <typename T, bool ENTROPY>
-__global__ void __launch_bounds__(kGradThreads, kGradCtas) k_token_logprobs_grad(LogprobGradArgs a) {
+__device__ __noinline__ void whole_row_grad(const LogprobGradArgs& a, int64_t n) {
+    __shared__ StatSmem stat_smem;
+    const RowPart<T> p(a.row, n, 0, kWholeRow);
+    const float c2 = a.row.c2, inv_tau = a.row.inv_tau;
+    const Stat st = whole_row_stats<kGradThreads>(p, stat_smem, c2);
+    const Slope<T> slope(a, n, ENTROPY, a.status);
+    const int v_id = slope.vector(p);
+    const bool empty = st.m == neg_inf();
+    const float ln_s = logf(st.s), inv_s = 1.0f / st.s;
+    stream_map<kGradThreads>(p, static_cast<T*>(a.out) + n * a.ld_out, [&](int v, uint4 w) {
+        float f[Elem<T>::E];
+        Elem<T>::unpack(w, f);
+#pragma unroll
+        for (int e = 0; e < Elem<T>::E; ++e) {
+            const float q = empty ? 0.0f : inv_s * exp2_fast(max_nan(exponent(f[e], st.m, c2), -150.0f));
+            f[e] = q == 0.0f ? 0.0f : q * fmaf(slope.k1, fmaf(f[e] - st.m, inv_tau, -ln_s), slope.k0);
+        }
+        if (v == v_id) slope.add_token(p, v, f);
+        return Elem<T>::pack(f);
+    });
+}
+
+// One CTA per piece of a row, or one for a row whose lse does not hold its sum.
+template <typename T, bool ENTROPY>
+__global__ void __launch_bounds__(kGradThreads, kGradCtas) k_token_logprobs_grad(const __grid_constant__ LogprobGradArgs a) {
     constexpr int E = Elem<T>::E;
     const int64_t n = blockIdx.x / a.tiles;
     const unsigned tile = blockIdx.x % a.tiles;
-    const RowPart<T> p(a.row, n, tile);
-    const int64_t id = load_id(a.ids, a.id64, n, a.row.V, tile == 0 ? a.status : nullptr);
     const float lse = __ldg(a.lse + n), inv_tau = a.row.inv_tau;
-    const float g = a.g_logprobs ? __ldg(a.g_logprobs + n) : 0.0f;
-    const float h = ENTROPY ? __ldg(a.g_entropy + n) : 0.0f;
-    const float H = ENTROPY ? __ldg(a.entropy + n) : 0.0f;
-    // d = p (k0 + k1 log p), and `token` more for the token; log p = y - lse in
-    // natural units, so that neither the rounding of lse * log2(e) nor that of
-    // 1 / temperature scales the row
-    const float token = g * inv_tau;
-    const float k1 = -h * inv_tau, k0 = fmaf(k1, H, id >= 0 ? -token : 0.0f);
-    const int v_id = id >= 0 ? static_cast<int>((id + p.shift) / E) : -1;
-    const bool usual = may_floor(lse, inv_tau);
-    T* out = static_cast<T*>(a.out) + n * a.ld_out;
-    stream_map<kGradThreads>(p, out, [&](int v, uint4 w) {
-        float f[E];
-        if (usual) {                        // masked entries at -2^60: p is 0 and log p finite
-            Elem<T>::unpack(floored<T>(w), f);
+    if (!lse_holds(lse)) {
+        if (tile == 0) whole_row_grad<T, ENTROPY>(a, n);
+        return;
+    }
+    const RowPart<T> p(a.row, n, tile);
+    const Slope<T> slope(a, n, ENTROPY, tile == 0 ? a.status : nullptr);
+    const int v_id = slope.vector(p);
+    const float k0 = slope.k0, k1 = slope.k1;
+    stream_map<kGradThreads>(p, static_cast<T*>(a.out) + n * a.ld_out, [&](int v, uint4 w) {
+        float f[E];                         // masked entries at -2^60: p is 0 and log p finite
+        Elem<T>::unpack(floored<T>(w), f);
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const uint64_t lp = log_prob_pair(pair(f[e], f[e + 1]), lse, inv_tau, a.inv_tau_low);
-                float y0, y1;
-                unpair(pair_mul(lp, pair(kLog2e, kLog2e)), y0, y1);
-                const uint64_t slope = ENTROPY ? pair_fma(lp, pair(k1, k1), pair(k0, k0)) : pair(k0, k0);
-                unpair(pair_mul(pair(exp2_fast(y0), exp2_fast(y1)), slope), f[e], f[e + 1]);
-            }
-        } else {                            // nothing but masked entries (p = 0), huge logits, or NaN
-            Elem<T>::unpack(w, f);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float lp = log_prob_from(f[e], lse, inv_tau, a.inv_tau_low);
-                const float q = lse == neg_inf() ? 0.0f : exp2_fast(max_nan(lp * kLog2e, -150.0f));
-                f[e] = q == 0.0f ? 0.0f : q * fmaf(k1, lp, k0);
-            }
+        for (int e = 0; e < E; e += 2) {
+            // log p = y - lse in natural units, so that neither the rounding of
+            // lse * log2(e) nor that of 1 / temperature scales the row
+            const uint64_t lp = log_prob_pair(pair(f[e], f[e + 1]), lse, inv_tau, a.inv_tau_low);
+            float y0, y1;
+            unpair(pair_mul(lp, pair(kLog2e, kLog2e)), y0, y1);
+            const uint64_t d = ENTROPY ? pair_fma(lp, pair(k1, k1), pair(k0, k0)) : pair(k0, k0);
+            unpair(pair_mul(pair(exp2_fast(y0), exp2_fast(y1)), d), f[e], f[e + 1]);
         }
-        if (v == v_id) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (p.index(v, e) == id) f[e] += token;
-        }
+        if (v == v_id) slope.add_token(p, v, f);
         return Elem<T>::pack(f);
     });
 }
@@ -502,6 +541,7 @@ int token_logprobs_grad(const void* logits, gc_dtype dtype, int64_t ld, const vo
     if (sms < 1) return GC_ERR_CUDA;
     LogprobGradArgs a = {};
     a.row.x = logits, a.row.ld = ld, a.row.N = N, a.row.V = static_cast<int>(V);
+    a.row.c2 = static_cast<float>(1.4426950408889634 / temperature);
     split_inverse(temperature, &a.row.inv_tau, &a.inv_tau_low);
     a.ids = ids, a.id64 = id_type == GC_I64;
     a.lse = lse, a.entropy = entropy, a.g_logprobs = g_logprobs, a.g_entropy = g_entropy;

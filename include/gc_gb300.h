@@ -859,9 +859,9 @@ GC_API size_t embed_grad_workspace_bytes(int64_t T, int64_t V, int64_t D);
  *   top_ids[n][], top_logprobs[n][]
  *                = the K entries with the largest x, largest first, equal
  *                  logits in order of their index (NaN counts as largest)
- * The row is read once.  lse is rounded to fp32: a gradient taken from it
- * carries that rounding, which shows where |lse| is above about 10^4 (a row of
- * the type's lowest values).
+ * The row is read once.  lse is rounded to fp32, so far from zero it holds
+ * less of the sum than logprobs, entropy and top_logprobs do, which are formed
+ * before (-1e9 + log V is -1e9); it is infinite where it leaves fp32's range.
  *
  *   logits     device [N][ld] of `dtype`
  *   ids        device [N] of `id_type`
@@ -885,10 +885,14 @@ GC_API int token_logprobs(const void *logits, gc_dtype dtype, int64_t ld,
  * g_entropy[n] * entropy[n] with respect to the logits:
  *   dlogits[n][j] = (g_logprobs[n] * ([j == ids[n]] - p_j)
  *                    - g_entropy[n] * p_j * (log p_j + entropy[n])) / temperature
- * (an absent token has no g_logprobs term), in fp32, rounded once.
+ * (an absent token has no g_logprobs term), in fp32, rounded once.  p comes
+ * from lse where |lse| < 1024 (whose rounding is then at most 2^-15 of p);
+ * other rows are read once more for their own maximum and sum, so a row filled
+ * with one mask value is uniform, whatever the value.
  *
- *   lse, entropy      device fp32 [N], from token_logprobs; entropy may be
- *                     NULL when g_entropy is
+ *   lse, entropy      device fp32 [N], from token_logprobs on the same logits
+ *                     at the same temperature; entropy may be NULL when
+ *                     g_entropy is
  *   g_logprobs, g_entropy
  *                     device fp32 [N]; either may be NULL (zero), not both
  *   dlogits           device [N][ld_out] of `dtype`, written; may be the
@@ -933,7 +937,7 @@ GC_API int distill_loss(const void *logits, gc_dtype dtype, int64_t ld,
  * the student's logits, from distill_loss's lse:
  *   dlogits[n][j] = weights[n] * tau * (p_j - sum over k with top_ids_k == j of q_k)
  * in fp32, rounded once; exact zeros where weights[n] is 0 or the row has no
- * mass.
+ * mass.  Rows with |lse| >= 1024 are read once more, as in token_logprobs_grad.
  *
  *   weights     device fp32 [N] (the upstream gradient of each row's loss)
  *   dlogits     device [N][ld_out] of `dtype`, written; may be the logits
