@@ -158,7 +158,7 @@ __device__ __forceinline__ void load_student(const Teacher& t, const T* row, int
 #pragma unroll
     for (int i = 0; i < GC_MAX_TOP / 32; ++i) {
         const int k = (threadIdx.x & 31) + 32 * i;
-        x[i] = k < K && t.id[k] >= 0 ? Elem<T>::load_plain(row + t.id[k]) : 0.0f;
+        x[i] = k < K && t.id[k] >= 0 ? Elem<T>::load_before(row + t.id[k]) : 0.0f;
     }
 }
 
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kTeacherThreads, kStepCtas) k_distill_loss_gra
         n_own = collect_own(own, teacher, a.K, p.index(p.v0, 0), p.index(p.v1, 0));
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            if (lane + 32 * i < n_own) x_own[i] = Elem<T>::load_plain(p.row + own.id[lane + 32 * i]);
+            if (lane + 32 * i < n_own) x_own[i] = Elem<T>::load_before(p.row + own.id[lane + 32 * i]);
     }
     const Stat cta = block_stats<kRowThreads>(stat_smem, mine, c2);
     cluster_started(parts);
@@ -362,7 +362,7 @@ struct PartEntries {
 #pragma unroll
         for (int i = 0; i < GC_MAX_TOP / 32; ++i) {
             const int k = (threadIdx.x & 31) + 32 * i;
-            if (k < n_own) x[i] = Elem<T>::load_plain(p.row + own.id[k]);
+            if (k < n_own) x[i] = Elem<T>::load_before(p.row + own.id[k]);
         }
     }
 };

@@ -557,7 +557,7 @@ __device__ __forceinline__ void shared_row(const GradArgs& a, TO* out, int64_t m
         for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
 #pragma unroll 8
         for (int64_t k = from; k <= to; k += step) {
-            const float4 x = __ldcg(place(k)), y = __ldcg(place(k) + 1);
+            const float4 x = load_ordered(place(k)), y = load_ordered(place(k) + 1);
             sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
             sum[4] += y.x, sum[5] += y.y, sum[6] += y.z, sum[7] += y.w;
         }

@@ -41,7 +41,32 @@ int allow_smem(Kernel* kernel, size_t smem, size_t most) {
 
 // ---------------------------------------------------------------- elements
 
-// A 16-byte vector holds E elements of T, read and written as floats.
+// Reads of memory that this kernel also writes, its other threads and CTAs among
+// them: volatile, so that the compiler keeps them on their side of a barrier (a
+// logit read before its gradient takes its place, a part of a sum read after the
+// counter said that it is there).  From L2, where other SMs' writes are.
+__device__ __forceinline__ float load_ordered(const float* p) {
+    float x;
+    asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(x) : "l"(__cvta_generic_to_global(p)) : "memory");
+    return x;
+}
+__device__ __forceinline__ unsigned short load_ordered(const unsigned short* p) {
+    unsigned short x;
+    asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(x) : "l"(__cvta_generic_to_global(p)) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 load_ordered(const float4* p) {
+    float4 x;
+    asm volatile("ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "l"(__cvta_generic_to_global(p))
+                 : "memory");
+    return x;
+}
+
+// A 16-byte vector holds E elements of T, read and written as floats.  load() is
+// of memory that the kernel only reads, load_plain() of elements that this
+// thread alone writes, load_before() of what others write after a barrier.
 template <typename T>
 struct Elem;
 
@@ -50,6 +75,7 @@ struct Elem<float> {
     static constexpr int E = 4;
     static __device__ __forceinline__ float load(const float* p) { return __ldg(p); }
     static __device__ __forceinline__ float load_plain(const float* p) { return __ldcg(p); }
+    static __device__ __forceinline__ float load_before(const float* p) { return load_ordered(p); }
     static __device__ __forceinline__ float round_to(float x) { return x; }
     static __device__ __forceinline__ void unpack(uint4 w, float (&f)[4]) {
         f[0] = __uint_as_float(w.x);
@@ -70,6 +96,9 @@ struct Elem<__nv_bfloat16> {
     }
     static __device__ __forceinline__ float load_plain(const __nv_bfloat16* p) {
         return bf16lo(__ldcg(reinterpret_cast<const unsigned short*>(p)));
+    }
+    static __device__ __forceinline__ float load_before(const __nv_bfloat16* p) {
+        return bf16lo(load_ordered(reinterpret_cast<const unsigned short*>(p)));
     }
     static __device__ __forceinline__ __nv_bfloat16 round_to(float x) { return __float2bfloat16_rn(x); }
     static __device__ __forceinline__ void unpack(uint4 w, float (&f)[8]) {
