@@ -224,6 +224,8 @@ constexpr int kStepCtas = 4;                // resident per SM
 
 // Barrier 1: the row's threads arrive, the teacher's warp waits for them.
 __device__ __forceinline__ void rows_arrive() { asm volatile("bar.arrive 1, %0;" ::"n"(kTeacherThreads) : "memory"); }
+// Barrier 2: both wait for each other.
+__device__ __forceinline__ void entries_ready() { asm volatile("bar.sync 2, %0;" ::"n"(kTeacherThreads) : "memory"); }
 __device__ __forceinline__ void teacher_wait() { asm volatile("bar.sync 1, %0;" ::"n"(kTeacherThreads) : "memory"); }
 
 // Writes g p = gs 2^(c2 (x - m)) over a part of a row; zeros where it has none.
@@ -409,26 +411,24 @@ __global__ void __launch_bounds__(kTeacherThreads, kGradCtas) k_distill_grad(con
     T* out = static_cast<T*>(a.out) + n * a.ld_out;
     const bool rows = threadIdx.x < kRowThreads, in_place = a.out == a.row.x;
     const float g = weight * a.tau;
-    PartEntries<T> entries;
-    if (!rows) {
-        entries.find(a, n, p, teacher, own, tile == 0 ? a.status : nullptr);
-        if (in_place) entries.gather(p, own);           // before any of them is overwritten
-    }
-    __syncthreads();
-    if (!lse_holds(lse) && weight != 0.0f) {            // without a weight all are zeros
-        if (tile == 0) whole_row_grad<T>(a, n, teacher, own);
-        return;
-    }
-    const bool zero = weight == 0.0f || !teacher.mass;
-    // log p = y - lse in natural units, so that neither the rounding of
-    // lse * log2(e) nor that of 1 / tau scales the row
+    // a row without a weight is zeros, whatever its lse
+    const bool holds = lse_holds(lse) || weight == 0.0f;
     if (rows) {
-        stream_map<kRowThreads>(p, out, [&](int, uint4 w) {
+        bool zero = false;
+        auto go = [&]() {                               // the teacher's entries are there
+            entries_ready();
+            if (!holds) return false;
+            zero = weight == 0.0f || !teacher.mass;
+            return true;
+        };
+        stream_map<kRowThreads>(p, out, go, [&](int, uint4 w) {
             float f[E];
             if (zero) return make_uint4(0, 0, 0, 0);
             Elem<T>::unpack(floored<T>(w), f);          // masked entries at -2^60: p is 0
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
+                // log p = y - lse in natural units, so that neither the rounding of
+                // lse * log2(e) nor that of 1 / tau scales the row
                 const uint64_t lp = log_prob_pair(pair(f[e], f[e + 1]), lse, inv_tau, a.inv_tau_low);
                 float y0, y1;
                 unpair(pair_mul(lp, pair(kLog2e, kLog2e)), y0, y1);
@@ -436,12 +436,19 @@ __global__ void __launch_bounds__(kTeacherThreads, kGradCtas) k_distill_grad(con
             }
             return Elem<T>::pack(f);
         });
-        rows_arrive();
+        if (holds) rows_arrive();
     } else {
-        if (!in_place) entries.gather(p, own);
-        correct_entries(own, entries.n_own, zero, entries.x, out, g,
-                        [&](float x) { return g * exp2_fast(log_prob_from(x, lse, inv_tau, a.inv_tau_low) * kLog2e); });
+        PartEntries<T> entries;
+        entries.find(a, n, p, teacher, own, tile == 0 ? a.status : nullptr);
+        if (in_place) entries.gather(p, own);           // before any of them is overwritten
+        entries_ready();
+        if (holds) {
+            if (!in_place) entries.gather(p, own);
+            correct_entries(own, entries.n_own, weight == 0.0f || !teacher.mass, entries.x, out, g,
+                            [&](float x) { return g * exp2_fast(log_prob_from(x, lse, inv_tau, a.inv_tau_low) * kLog2e); });
+        }
     }
+    if (!holds && tile == 0) whole_row_grad<T>(a, n, teacher, own);
 }
 
 // ---------------------------------------------------------------- host

@@ -100,9 +100,11 @@ __device__ __forceinline__ Stat whole_row_stats(const RowPart<T> p, StatSmem& sm
 
 // Writes f(v, vector v) to the same places of `out` for every vector of the
 // part, the next unit's vectors read before the present one's arithmetic.
-// `out` may be the row itself.  Threads below TH call it.
-template <int TH, typename T, typename F>
-__device__ __forceinline__ void stream_map(const RowPart<T>& p, T* out, F f) {
+// `out` may be the row itself.  go() is called once the first unit's vectors are
+// on their way; false ends the call with nothing written.  Threads below TH call
+// it.
+template <int TH, typename T, typename Go, typename F>
+__device__ __forceinline__ void stream_map(const RowPart<T>& p, T* out, Go go, F f) {
     constexpr int E = RowPart<T>::E;
     const bool same = row_shift(out) == p.shift;
     uint4* dst = reinterpret_cast<uint4*>(out - p.shift);
@@ -127,6 +129,7 @@ __device__ __forceinline__ void stream_map(const RowPart<T>& p, T* out, F f) {
             if (from + k * TH < p.i1) next[k] = __ldcs(p.vectors() + from + k * TH);
     };
     fetch(v);
+    if (!go()) return;
     if (threadIdx.x == 0 && p.v0 < p.i0) store(p.v0, f(p.v0, p.load(p.v0)));
     if (threadIdx.x == 1 && p.i1 < p.v1) store(p.i1, f(p.i1, p.load(p.i1)));
     if (same) {                             // complete units without a look at their ends
@@ -149,6 +152,11 @@ __device__ __forceinline__ void stream_map(const RowPart<T>& p, T* out, F f) {
         for (int k = 0; k < kBatch; ++k)
             if (v + k * TH < p.i1) store(v + k * TH, f(v + k * TH, w[k]));
     }
+}
+
+template <int TH, typename T, typename F>
+__device__ __forceinline__ void stream_map(const RowPart<T>& p, T* out, F f) {
+    stream_map<TH>(p, out, []() { return true; }, f);
 }
 
 // Vectors per CTA of a kernel that maps rows piece by piece, `slots` CTAs
