@@ -793,10 +793,12 @@ GC_API int saps_mask_compact_noalloc(int64_t n, double p, uint64_t seed_t,
  * *d_status (a device int that the caller has zeroed; NULL to ignore).
  * `temperature` divides the logits and lies in 1e-6 .. 1e6.
  *
- * Logits of -inf are masked entries: probability 0, gradient 0.  A row with
- * nothing but -inf has no distribution: its lse, and every log probability in
- * it, is -inf, its entropy 0, every probability 0.  A row with a NaN or +inf
- * has NaN for all of these.  Every result is a fixed function of the inputs
+ * Logits of -inf are masked entries: probability 0, and no gradient but the
+ * term of a given token, or of a teacher's entry, that lies there: its log
+ * probability is -inf, and the formulas' [j == ids[n]] and q_k remain.  A row
+ * with nothing but -inf has no distribution: its lse, and every log probability
+ * in it, is -inf, its entropy 0, every probability 0 (its gradient is those
+ * terms alone).  A row with a NaN or +inf has NaN for all of these.  Every result is a fixed function of the inputs
  * and the device (no floating-point atomics).  The calls of this section may
  * come from several host threads at once; each needs buffers of its own.
  */

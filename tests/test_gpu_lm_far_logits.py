@@ -174,3 +174,39 @@ def test_gradients_of_many_rows_without_a_choice(N):
     p = softmax64(_from_max(x), 0.5)[3]
     p[:, 7] -= 1.0
     assert ((out.cpu().double() + 2 * p).abs() <= 2 * (p.abs() + 1e-9) * (sum_error(V) + 8 * U * 40)).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_given_tokens_at_masked_logits(dtype):
+    """The token's and the teacher's terms remain where the logit is -inf, in a usual row and in one of nothing else;
+    other masked places have no gradient."""
+    V, tau = 2500, 2.0
+    x = torch.randn(4, V, generator=torch.Generator().manual_seed(3)).to(dtype)
+    x[:, 100:200] = -INF
+    x[1] = x[3] = -INF
+    d = _device(x, 3, 1)
+    ids = torch.tensor([150, 150, 5, -1], device=DEV)
+    lp, H, lse = (torch.empty(4, device=DEV) for _ in range(3))
+    gc.token_logprobs(d, ids, lp, entropy=H, lse=lse, temperature=tau)
+    assert lp[0] == -INF and lp[1] == -INF and H[1] == 0 and lp[3] == 0
+    out = torch.full_like(d, 9.0)
+    g, h = torch.tensor([0.5, 0.25, 1.0, 4.0], device=DEV), torch.tensor([1.0, 8.0, 0.0, 8.0], device=DEV)
+    gc.token_logprobs_grad(d, ids, lse, H, g, h, out, temperature=tau)
+    out = out.cpu().float()
+    assert out[0, 150] == 0.25 and out[1, 150] == 0.125        # g / tau, exact in both types
+    masked = torch.isinf(x)
+    masked[0, 150] = masked[1, 150] = False
+    assert not out[masked].any() and torch.isfinite(out).all() and out[0, 5] != 0
+
+    top = torch.tensor([[150, 5]] * 4, dtype=torch.int32, device=DEV)
+    t, w, loss = torch.zeros(4, 2, device=DEV), torch.ones(4, device=DEV), torch.empty(4, device=DEV)
+    gc.distill_loss(d, top, t, loss, lse, temperature=tau)
+    assert (loss == INF).all()
+    masked[:, 150] = masked[:, 5] = False
+    for call in (lambda: gc.distill_grad(d, top, t, lse, w, out, temperature=tau),
+                 lambda: gc.distill_loss_grad(d, top, t, w, loss, out, temperature=tau)):
+        out = torch.full_like(d, 9.0)
+        call()
+        out = out.cpu().float()
+        assert (out[:, 150] == -1.0).all() and (out[[1, 3], 5] == -1.0).all()      # -w tau q
+        assert not out[masked].any() and torch.isfinite(out).all() and out[0, 6] > 0
