@@ -123,11 +123,17 @@ __global__ void __launch_bounds__(kThreads) k_embed_lookup(LookupArgs a) {
 //   many:       a first launch, a CTA per tile of kTile tokens, sorts each tile
 //               by class and writes the tokens (place in the tile, number of
 //               the id in its class) with the classes' starts.
-// Reading everything costs B times the ids, the second launch about 4 us.  The
-// whole gradient, one launch against two: 33 and 35 us at 2000 tokens into
-// 131072 x 256, 40 and 37 at 6000, 41 and 38 at 10000; 18 and 21 at 3000 into
-// 750 x 1024, 21.6 and 23.5 at 6000 into 1500 x 1024, 24.3 and 25.7 at 10000
-// into 2500 x 1024.
+// Reading everything costs B times the ids, the second launch 2 to 5 us.  Where
+// the two cross depends on the table, since the zeroing of its last rows hides
+// more of the longer sort: the whole gradient, cold L2, one launch against two,
+//   tokens              2000        4000        6000        8000       10000
+//   2500 x 1024      21.2  24.2  23.3  28.3  25.3  28.3  29.3  30.4  33.4  34.5
+//   32003 x 1001     35.5  38.5  43.7  45.7  45.7  46.7  49.8  48.8  51.9  50.8
+//   50000 x 768 bf16 25.2  30.3  28.4  31.4  31.4  32.4  33.4  32.4  35.5  34.4
+//   131072 x 256     33.4  36.5  35.6  36.5  39.6  38.5  41.6  38.5  41.7  38.5
+//   131072 x 2048     177   176   181   178   184   182   189   184   194   186
+// The rule goes by the tokens alone, in the middle of the crossings: at its
+// bound it gives up 2 us of 184 into the largest, 3 us of 28 into the smallest.
 // Both launches place tokens the same way: a warp's tokens follow one another,
 // per (warp, key) counts summed over warps and keys give each warp its first
 // place for each key, and within 32 tokens a match gives the rank.

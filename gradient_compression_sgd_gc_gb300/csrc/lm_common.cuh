@@ -1,7 +1,7 @@
 // lm_common.cuh -- what the language-model kernels (embed.cu, logprobs.cu,
-// distill.cu) share: 16-byte vectors of either element type, token ids, the
-// base-2 exponential, and the on-chip row of logits with its softmax
-// statistics.
+// distill.cu) share: argument checks, the limit of dynamic shared memory,
+// 16-byte vectors of either element type, token ids, the base-2 exponential and
+// log probabilities from a stored lse.
 #pragma once
 
 #include "gc_common.cuh"

@@ -149,8 +149,9 @@ __device__ __noinline__ void descend(const RowPart<T> p, TopSmem& sm, uint64_t* 
 
 // The K best entries of this CTA's part where too many are not below `low` to
 // be collected: the K-th key by bisection between `low`, which K entries reach,
-// and the largest key, then the entries above it and its first ties.  Some 20
-// readings of the part, whatever the values.
+// and the largest key, a reading for each bit of their distance, then the
+// entries above it and its first ties: some 20 readings of the part where the
+// values lie close together, 35 at most (one key far above a plateau of ties).
 template <int TH, typename T>
 __device__ __noinline__ void exact_top(const RowPart<T> p, TopSmem& sm, uint64_t* cand, uint32_t low, uint32_t high, int K) {
     const int lane = threadIdx.x & 31;
