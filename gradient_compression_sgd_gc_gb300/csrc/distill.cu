@@ -339,7 +339,6 @@ struct DistillGradArgs {
     unsigned tiles;                         // CTAs per row
     int K;
     float tau;
-    float inv_tau_low;                      // what 1 / tau is above row.inv_tau
     const float* lse;
     const float* weights;
     void* out;
@@ -429,7 +428,7 @@ __global__ void __launch_bounds__(kTeacherThreads, kGradCtas) k_distill_grad(con
             for (int e = 0; e < E; e += 2) {
                 // log p = y - lse in natural units, so that neither the rounding of
                 // lse * log2(e) nor that of 1 / tau scales the row
-                const uint64_t lp = log_prob_pair(pair(f[e], f[e + 1]), lse, inv_tau, a.inv_tau_low);
+                const uint64_t lp = log_prob_pair(pair(f[e], f[e + 1]), lse, inv_tau, a.row.inv_tau_low);
                 float y0, y1;
                 unpair(pair_mul(lp, pair(kLog2e, kLog2e)), y0, y1);
                 unpair(pair_mul(pair(exp2_fast(y0), exp2_fast(y1)), pair(g, g)), f[e], f[e + 1]);
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(kTeacherThreads, kGradCtas) k_distill_grad(con
         if (holds) {
             if (!in_place) entries.gather(p, own);
             correct_entries(own, entries.n_own, weight == 0.0f || !teacher.mass, entries.x, out, g,
-                            [&](float x) { return g * exp2_fast(log_prob_from(x, lse, inv_tau, a.inv_tau_low) * kLog2e); });
+                            [&](float x) { return g * exp2_fast(log_prob_from(x, lse, inv_tau, a.row.inv_tau_low) * kLog2e); });
         }
     }
     if (!holds && tile == 0) whole_row_grad<T>(a, n, teacher, own);
@@ -503,7 +502,7 @@ DistillArgs distill_args(const void* logits, int64_t ld, const int32_t* top_ids,
     DistillArgs a = {};
     a.row.x = logits, a.row.ld = ld, a.row.N = N, a.row.V = static_cast<int>(V);
     a.row.c2 = static_cast<float>(1.4426950408889634 / temperature);
-    a.row.inv_tau = static_cast<float>(1.0 / temperature);
+    split_inverse(temperature, &a.row.inv_tau, &a.row.inv_tau_low);
     a.top_ids = top_ids, a.top_logits = top_logits, a.K = K, a.tau = static_cast<float>(temperature);
     a.loss = loss;
     a.status = d_status;
@@ -570,7 +569,7 @@ int distill_grad(const void* logits, gc_dtype dtype, int64_t ld, const int32_t* 
     DistillGradArgs a = {};
     a.row.x = logits, a.row.ld = ld, a.row.N = N, a.row.V = static_cast<int>(V);
     a.row.c2 = static_cast<float>(1.4426950408889634 / temperature);
-    split_inverse(temperature, &a.row.inv_tau, &a.inv_tau_low);
+    split_inverse(temperature, &a.row.inv_tau, &a.row.inv_tau_low);
     a.top_ids = top_ids, a.top_logits = top_logits, a.K = K;
     a.tau = static_cast<float>(temperature);
     a.lse = lse, a.weights = weights, a.out = dlogits, a.ld_out = ld_out;

@@ -16,7 +16,7 @@ struct RowArgs {
     int V;
     int part;                               // vectors per CTA
     float c2;                               // log2(e) / temperature
-    float inv_tau;
+    float inv_tau, inv_tau_low;             // 1 / temperature, and what it is above the first
 };
 
 // ---------------------------------------------------------------- cluster
@@ -313,8 +313,10 @@ __device__ __forceinline__ float log_prob(const Stat& st, float ln_s, float x, c
     return st.m == neg_inf() ? neg_inf() : fmaf(x - st.m, a.inv_tau, -ln_s);
 }
 
+// With 1 / temperature in two terms, as the gradients take it: one alone is off
+// by up to 2^-24 of lse, twice lse's own rounding.
 __device__ __forceinline__ float row_lse(const Stat& st, float ln_s, const RowArgs& a) {
-    return st.m == neg_inf() ? neg_inf() : fmaf(st.m, a.inv_tau, ln_s);
+    return st.m == neg_inf() ? neg_inf() : fmaf(st.m, a.inv_tau, fmaf(st.m, a.inv_tau_low, ln_s));
 }
 
 // ---------------------------------------------------------------- launch

@@ -365,7 +365,6 @@ struct LogprobGradArgs {
     const void* ids;
     unsigned tiles;                         // CTAs per row
     int id64;
-    float inv_tau_low;                      // what 1 / temperature is above row.inv_tau
     const float* lse;
     const float* entropy;
     const float* g_logprobs;
@@ -453,7 +452,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas) k_token_logprobs_grad
         for (int e = 0; e < E; e += 2) {
             // log p = y - lse in natural units, so that neither the rounding of
             // lse * log2(e) nor that of 1 / temperature scales the row
-            const uint64_t lp = log_prob_pair(pair(f[e], f[e + 1]), lse, inv_tau, a.inv_tau_low);
+            const uint64_t lp = log_prob_pair(pair(f[e], f[e + 1]), lse, inv_tau, a.row.inv_tau_low);
             float y0, y1;
             unpair(pair_mul(lp, pair(kLog2e, kLog2e)), y0, y1);
             const uint64_t d = ENTROPY ? pair_fma(lp, pair(k1, k1), pair(k0, k0)) : pair(k0, k0);
@@ -518,7 +517,7 @@ int token_logprobs(const void* logits, gc_dtype dtype, int64_t ld, const void* i
     LogprobArgs a;
     a.row.x = logits, a.row.ld = ld, a.row.N = N, a.row.V = static_cast<int>(V), a.row.part = 0;
     a.row.c2 = static_cast<float>(1.4426950408889634 / temperature);
-    a.row.inv_tau = static_cast<float>(1.0 / temperature);
+    split_inverse(temperature, &a.row.inv_tau, &a.row.inv_tau_low);
     a.ids = ids, a.id64 = id_type == GC_I64, a.K = K;
     a.logprobs = logprobs, a.entropy = entropy, a.lse = lse, a.top_ids = top_ids, a.top_logprobs = top_logprobs;
     a.status = d_status;
@@ -543,7 +542,7 @@ int token_logprobs_grad(const void* logits, gc_dtype dtype, int64_t ld, const vo
     LogprobGradArgs a = {};
     a.row.x = logits, a.row.ld = ld, a.row.N = N, a.row.V = static_cast<int>(V);
     a.row.c2 = static_cast<float>(1.4426950408889634 / temperature);
-    split_inverse(temperature, &a.row.inv_tau, &a.inv_tau_low);
+    split_inverse(temperature, &a.row.inv_tau, &a.row.inv_tau_low);
     a.ids = ids, a.id64 = id_type == GC_I64;
     a.lse = lse, a.entropy = entropy, a.g_logprobs = g_logprobs, a.g_entropy = g_entropy;
     a.out = dlogits, a.ld_out = ld_out;

@@ -210,3 +210,29 @@ def test_given_tokens_at_masked_logits(dtype):
         out = out.cpu().float()
         assert (out[:, 150] == -1.0).all() and (out[[1, 3], 5] == -1.0).all()      # -w tau q
         assert not out[masked].any() and torch.isfinite(out).all() and out[0, 6] > 0
+
+
+@pytest.mark.parametrize("tau", [0.9, 7.0, 1.7, 0.3])
+def test_lse_below_1024_is_rounded_once(tau):
+    """lse within its own rounding (2^-15 from 512 to 1024) and the sum's error, at temperatures whose inverse is not
+    an fp32 number; so the probabilities that a gradient forms from it sum to one as closely."""
+    N, V = 300, 40
+    gen = torch.Generator().manual_seed(5)
+    x = torch.randn(N, V, generator=gen) + (torch.linspace(520, 1000, N) * tau)[:, None]
+    x[::2] *= -1.0
+    d, ids = _device(x, 1, 3), torch.randint(0, V, (N,), generator=gen).to(DEV)
+    lp, lse, loss = (torch.empty(N, device=DEV) for _ in range(3))
+    top, t = ids[:, None].int().contiguous(), torch.zeros(N, 1, device=DEV)
+    m = x.double().max(1).values
+    want = m / tau + torch.log(torch.exp(_from_max(x) / tau).sum(1))
+    tol = 2.0 ** -15 + sum_error(V)
+    for call in (lambda: gc.token_logprobs(d, ids, lp, lse=lse, temperature=tau),
+                 lambda: gc.distill_loss(d, top, t, loss, lse, temperature=tau)):
+        lse.zero_()
+        call()
+        assert ((lse.cpu().double() - want).abs() <= tol).all()
+    out, g = torch.empty_like(d), torch.ones(N, device=DEV)
+    gc.token_logprobs_grad(d, ids, lse, None, g, None, out, temperature=tau)
+    assert (out.cpu().double().sum(1).abs() * tau <= tol + 64 * U).all()
+    gc.distill_grad(d, top, t, lse, g, out, temperature=tau)
+    assert (out.cpu().double().sum(1).abs() / tau <= tol + 64 * U).all()
