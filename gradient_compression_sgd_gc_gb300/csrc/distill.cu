@@ -5,8 +5,8 @@
 //   loss = tau^2 sum_k q_k (log q_k - log p[id_k])
 //   d_j  = w tau (p_j - sum_{k: id_k = j} q_k)
 //
-// The loss reads each logit once; the gradient reads and writes each once, and
-// so does, in memory, the loss with its gradient: its second reading of a row
+// The loss reads each logit once; the gradient reads and writes each once (rows
+// with |lse| >= 1024 are read twice), and so does, in memory, the loss with its gradient: its second reading of a row
 // comes from L2.
 #include "logit_stream.cuh"
 

@@ -6,7 +6,7 @@
 //   d = (g (onehot - p) - h p (log p + H)) / tau
 //
 // The forward pass reads each logit once from memory, the gradient reads and
-// writes each once.
+// writes each once (rows with |lse| >= 1024 are read twice).
 #include "logit_stream.cuh"
 
 namespace gc {
