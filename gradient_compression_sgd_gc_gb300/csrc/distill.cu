@@ -224,9 +224,9 @@ constexpr int kStepCtas = 4;                // resident per SM
 
 // Barrier 1: the row's threads arrive, the teacher's warp waits for them.
 __device__ __forceinline__ void rows_arrive() { asm volatile("bar.arrive 1, %0;" ::"n"(kTeacherThreads) : "memory"); }
+__device__ __forceinline__ void teacher_wait() { asm volatile("bar.sync 1, %0;" ::"n"(kTeacherThreads) : "memory"); }
 // Barrier 2: both wait for each other.
 __device__ __forceinline__ void entries_ready() { asm volatile("bar.sync 2, %0;" ::"n"(kTeacherThreads) : "memory"); }
-__device__ __forceinline__ void teacher_wait() { asm volatile("bar.sync 1, %0;" ::"n"(kTeacherThreads) : "memory"); }
 
 // Writes g p = gs 2^(c2 (x - m)) over a part of a row; zeros where it has none.
 template <typename T>
